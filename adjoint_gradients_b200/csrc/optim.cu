@@ -242,8 +242,8 @@ __device__ __forceinline__ float2 round_first(float2 x, float2 inv, const uint32
 // Second moment: a lies between lo and lo + d (d the spacing of its binade, 2^-9
 // below 2^-6); up where (a - lo) (a + lo) > u d (2 lo + d), the chance that
 // keeps the mean of a^2.  The right side is exact (16 + 5 bits), the left one
-// rounded twice.  Where lo = 0 the right side is taken as 0: every positive r
-// rounds up and none vanishes.
+// rounded twice.  Where lo = 0 the right side is taken as -a: the left one may
+// underflow to 0, but every positive r rounds up and none vanishes.
 __device__ __forceinline__ float2 round_second(float2 r, float2 inv, const uint32_t (&y)[2]) {
   const float2 a = mul2(r, inv);
   auto binade = [](float t) { return __uint_as_float(max(__float_as_uint(t) & 0x7f800000u, 121u << 23)); };
@@ -253,7 +253,7 @@ __device__ __forceinline__ float2 round_second(float2 r, float2 inv, const uint3
   const float2 left = mul2(add2(a, neg2(lo)), add2(a, lo));
   auto uniform = [](uint32_t w) { return __uint_as_float(__byte_perm(w, 0x41800000u, 0x7632)); };  // 16 + u / 8
   const float2 u = add2(make_float2(uniform(y[0]), uniform(y[1])), both(-16.f));
-  const float2 right = mul2(mul2(u, e), fma2(lo, both(2.f), d)), most = mul2(lo, both(0x1p40f));
+  const float2 right = mul2(mul2(u, e), fma2(lo, both(2.f), d)), most = fma2(lo, both(0x1p40f), neg2(a));
   auto above = [](float l, float r0, float r1) {
     float one;
     asm("set.gt.f32.f32 %0, %1, %2;" : "=f"(one) : "f"(l), "f"(fminf(r0, r1)));

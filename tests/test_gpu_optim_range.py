@@ -1,0 +1,35 @@
+"""8-bit optimiser states where one block holds magnitudes that are far apart: what
+the codes' definition says must hold to the ends of fp32's range."""
+import numpy as np
+import pytest
+
+from test_gpu_optim import BETAS, EPS, codes_in_fp32, optim, random_bits
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+F = np.float32
+
+
+def second(g):
+    """sqrt((1 - beta2) g^2), the root of a first step's second moment, in fp32."""
+    return np.sqrt((g * g) * F(1 - BETAS[1]))
+
+
+# one launch and the general kernel; whole blocks, and the last one ragged
+@pytest.mark.parametrize("n", [256, 300, 65_536, 70_001])
+@pytest.mark.parametrize("top,low", [(1e10, -22), (1e19, -22), (1.0, -22), (1e-3, -24)])
+def test_a_positive_second_moment_never_becomes_zero(n, top, low):
+    # a block's largest fixes the scale; the others go down to where g^2 vanishes in fp32
+    rng = np.random.default_rng(n)
+    g = (10.0 ** rng.uniform(low, np.log10(top), n)).astype(F) * rng.choice([-1, 1], n).astype(F)
+    g[::256] = top
+    seed = 5
+    opt = optim().AdamW([torch.ones(n, device="cuda")], betas=BETAS, eps=EPS, state="8bit", seed=seed, weight_decay=0.0)
+    opt.step([torch.from_numpy(g).cuda()], lr=0.1)
+    r = second(g)
+    got = opt.v.float().cpu().numpy()[:n]
+    assert (r == 0).any() and (r[got == 0] == 0).all(), np.abs(g[(got == 0) & (r > 0)]).max()
+    pad = np.zeros(-n % 256, F)
+    want, _ = codes_in_fp32(np.concatenate([r, pad]), random_bits(seed, 1, 0, n + len(pad)) >> np.uint32(16), True)
+    assert np.array_equal(got, want[:n])
