@@ -478,7 +478,8 @@ typedef enum { QML_F32 = 0, QML_F64 = 1, QML_BF16 = 2, QML_F16 = 3 } qml_dtype;
  * consecutive elements of a tensor sharing a float scale (their largest
  * magnitude / 448): value = code * scale, v = value^2.  Both round at random
  * to a neighbouring code, so that m and v are right in the mean (to 2^-16 of
- * the codes' spacing); a positive r never becomes 0.  The random bits depend
+ * the codes' spacing); a positive r never becomes 0, and where r is 0 (v
+ * vanishes in fp32) m is stored as 0.  The random bits depend
  * on the seed, the step, the tensor's place in the list and the element only.
  * Initial states are zeros (codes and scales).  A block that holds a NaN or
  * infinity reads back as NaN. */

@@ -33,3 +33,25 @@ def test_a_positive_second_moment_never_becomes_zero(n, top, low):
     pad = np.zeros(-n % 256, F)
     want, _ = codes_in_fp32(np.concatenate([r, pad]), random_bits(seed, 1, 0, n + len(pad)) >> np.uint32(16), True)
     assert np.array_equal(got, want[:n])
+
+
+@pytest.mark.parametrize("n", [65_536, 200_001])
+def test_a_first_moment_without_a_second_one_is_not_kept(n):
+    # g^2 vanishes in fp32 for all but each block's first element.  A first moment that
+    # rounds up to a code there would be divided by eps alone at the next step, and at
+    # the random number 0 everything positive rounds up.
+    seed = 2
+    first = np.arange(n) % 256 == 0
+    zero = ((random_bits(seed, 1, 0, n) & np.uint32(0xFFFF)) == 0) & ~first
+    assert zero.any()
+    g = np.where(first, 1.0, 1e-24 * np.where(np.arange(n) % 2, 1, -1)).astype(F)
+    assert (second(g)[~first] == 0).all()
+    p = torch.ones(n, device="cuda")
+    opt = optim().AdamW([p], betas=BETAS, eps=EPS, state="8bit", seed=seed, weight_decay=0.0)
+    for _ in range(3):
+        opt.step([torch.from_numpy(g).cuda()], lr=0.1)
+        m, v = (x.cpu().numpy() for x in opt.moments(0))
+        assert (v[~first] == 0).all() and (v[first] > 0).all() and (m[first] > 0).all()
+        assert (m[~first] == 0).all(), m[zero]
+        # lr m / eps of the moments before rounding: 0.1 * 1e-24 / 1e-8 a step, nothing in fp32
+        assert (p.cpu().numpy()[~first] == 1.0).all()
