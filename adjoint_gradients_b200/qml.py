@@ -197,6 +197,16 @@ def _current_stream(device: int | None = None) -> int:
     return _raw_stream(_current_device() if device is None else device)
 
 
+def _made_current(stream, device: int):
+    """Context in which `stream` (a torch stream, or a handle) is torch's current stream,
+    so that tensors made in it belong to that stream."""
+    import torch
+
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(getattr(stream, "cuda_stream", stream), device=device)
+    return torch.cuda.stream(stream)
+
+
 def _stream_handle(stream) -> int | None:
     if stream is None:
         return _current_stream()

@@ -1,0 +1,67 @@
+"""The optimiser's outputs and temporaries under captured graphs and other streams."""
+import math
+
+import pytest
+
+from test_gpu_optim import make, optim
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("sizes", [[24], [70_000, 300]])
+def test_replays_of_a_step_whose_norm_was_dropped_leave_other_tensors_alone(sizes):
+    params, grads = make(sizes, "fp32", "fp32", 30)
+    opt = optim().AdamW(params)
+    opt.step(grads, max_norm=1.0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        opt.step(grads, max_norm=1.0)  # the norm is dropped
+    for _ in range(40):
+        opt.grad_norm(grads)
+    others = [torch.full((1,), 7.0, device="cuda") for _ in range(400)]  # whatever small memory is free
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(float(x) == 7.0 for x in others)
+    assert opt.step_count == 4
+
+
+def test_norms_of_another_stream_belong_to_it():
+    params, grads = make([70_000], "fp32", "fp32", 31)
+    opt = optim().AdamW(params)
+    want = math.sqrt(float((grads[0].double() ** 2).sum()))
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):  # an object, a handle
+        side.wait_stream(torch.cuda.current_stream())
+        for call in (lambda: opt.step(grads, max_norm=1.0, stream=stream), lambda: opt.grad_norm(grads, stream=stream)):
+            norm = call()
+            side.synchronize()
+            assert float(norm) == pytest.approx(want, rel=1e-6)
+            at = norm.data_ptr()
+            del norm
+            torch.cuda.synchronize()
+            others = [torch.empty(1, device="cuda") for _ in range(300)]
+            assert at not in {x.data_ptr() for x in others}  # not for other streams' tensors
+    assert torch.cuda.current_stream() != side
+
+
+def test_a_captured_norm_is_the_graphs():
+    params, grads = make([24, 5003], "fp32", "fp32", 32)
+    opt = optim().AdamW(params)
+    opt.step(grads, max_norm=1.0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        norm = opt.step(grads, max_norm=1.0)
+        alone = opt.grad_norm(grads, grad_scale=2.0)
+    for k in range(3):
+        for g in grads:
+            g.mul_(1.5)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = math.sqrt(sum(float((g.double() ** 2).sum()) for g in grads))
+        assert float(norm) == pytest.approx(want, rel=1e-6) and float(alone) == pytest.approx(2 * want, rel=1e-6)
