@@ -206,12 +206,7 @@ class AdamW:
                 self._norms_of, self._norms = here, list(self._one.new_empty((64, 1)).unbind(0))
             return self._norms.pop()
         if norm is None:
-            import torch
-
-            with qml._made_current(stream, self._index):
-                norm = self._one.new_empty(1)
-            norm.record_stream(torch.cuda.current_stream(self._index))  # where the caller reads it
-            return norm
+            return qml._run_on(stream, self._index, lambda: self._one.new_empty(1))
         self._check_buffer(norm, self.real_dtype, 1, "the norm")
         return norm
 

@@ -207,6 +207,21 @@ def _made_current(stream, device: int):
     return torch.cuda.stream(stream)
 
 
+def _run_on(stream, device: int, call):
+    """call() with `stream` current: what it allocates belongs to that stream, and what it
+    drops may serve that stream's later work only.  The tensors it returns may be read and
+    dropped on the stream that is current now."""
+    import torch
+
+    reader = torch.cuda.current_stream(device)
+    with _made_current(stream, device):
+        out = call()
+    for t in out if isinstance(out, tuple) else (out,):
+        if t is not None:
+            t.record_stream(reader)
+    return out
+
+
 def _stream_handle(stream) -> int | None:
     if stream is None:
         return _current_stream()
@@ -516,19 +531,23 @@ class Context:
         backward, then opt (an optim.AdamW over [theta]) updates theta in place.
         psi and lam are working states (allocated when not given).  With a
         torch.distributed process group the ranks' gradients are averaged
-        before the update (on the current stream).  Returns (E, loss, gradient
-        norm or None)."""
-        if group is not None and stream is not None:
-            raise ValueError("with a process group, make the stream current instead of passing it")
+        before the update (on the current stream).  With `stream` everything runs
+        there: the inputs are ready in its order, and kept until it has read
+        them.  Returns (E, loss, gradient norm or None)."""
+        if stream is not None:
+            if group is not None:
+                raise ValueError("with a process group, make the stream current instead of passing it")
+            return _run_on(stream, self.device,
+                           lambda: self.train_step(theta, x, y, opt, psi=psi, lam=lam, lr=lr, max_norm=max_norm))
         B = x.shape[0]
-        psi, E = self.forward(theta, x, psi=psi, stream=stream)
-        g, loss = self.loss_seed(E, y, stream=stream)
-        grad = self.backward(theta, x, psi, self.new_state(B) if lam is None else lam, g, stream=stream)
+        psi, E = self.forward(theta, x, psi=psi)
+        g, loss = self.loss_seed(E, y)
+        grad = self.backward(theta, x, psi, self.new_state(B) if lam is None else lam, g)
         if group is not None:
             from .dp import average_gradients
 
             average_gradients(grad, group)
-        norm = opt.step([grad], lr=lr, max_norm=max_norm, stream=stream)
+        norm = opt.step([grad], lr=lr, max_norm=max_norm)
         return E, loss, norm
 
     @property

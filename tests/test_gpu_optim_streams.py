@@ -1,9 +1,11 @@
 """The optimiser's outputs and temporaries under captured graphs and other streams."""
 import math
 
+import numpy as np
 import pytest
 
-from test_gpu_optim import make, optim
+from adjoint_gradients_b200.inputs import random_case
+from test_gpu_optim import bits, make, optim, qml, same
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -65,3 +67,30 @@ def test_a_captured_norm_is_the_graphs():
         torch.cuda.synchronize()
         want = math.sqrt(sum(float((g.double() ** 2).sum()) for g in grads))
         assert float(norm) == pytest.approx(want, rel=1e-6) and float(alone) == pytest.approx(2 * want, rel=1e-6)
+
+
+@pytest.mark.parametrize("n,L,B,handle", [(6, 3, 5, False), (16, 12, 8, False), (16, 12, 8, True)])
+def test_training_steps_on_another_stream(n, L, B, handle):
+    # the current stream allocates and fills memory while the other one works: nothing of
+    # the step may lie in it
+    x, theta, y = (torch.from_numpy(a.astype(np.float32)).cuda() for a in random_case(88, B, n, L))
+    runs = []
+    for other in (False, True):
+        ctx = qml().Context(n, L, B, ckpt_block=2)
+        th = theta.clone()
+        opt = optim().AdamW([th], lr=0.05)
+        side = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        stream = (side.cuda_stream if handle else side) if other else None
+        outs = []
+        for _ in range(4):
+            outs.append(ctx.train_step(th, x, y, opt, max_norm=0.5, stream=stream))
+            if other:
+                noise = [torch.full_like(t, math.nan) for t in (ctx.new_state(B), ctx.new_state(B), theta, y, y[:1])
+                         for _ in range(3)]
+        torch.cuda.synchronize()
+        ctx.sync(stream)
+        opt.sync(stream)
+        runs.append(bits([th, opt.m, opt.v] + [t for o in outs for t in o]))
+    assert same(*runs)
+    assert len(noise) == 15
