@@ -528,12 +528,16 @@ class Context:
 
     def train_step(self, theta, x, y, opt, psi=None, lam=None, lr=None, max_norm=None, group=None, stream=None):
         """One training step on the mean squared loss: forward, loss, adjoint
-        backward, then opt (an optim.AdamW over [theta]) updates theta in place.
+        backward, then opt (an optim.AdamW over [theta], else ValueError) updates
+        theta in place.
         psi and lam are working states (allocated when not given).  With a
         torch.distributed process group the ranks' gradients are averaged
         before the update (on the current stream).  With `stream` everything runs
         there: the inputs are ready in its order, and kept until it has read
         them.  Returns (E, loss, gradient norm or None)."""
+        if len(opt.params) != 1 or opt.params[0].data_ptr() != theta.data_ptr() or \
+                opt.params[0].numel() != theta.numel():
+            raise ValueError("the optimiser holds other parameters than theta")
         if stream is not None:
             if group is not None:
                 raise ValueError("with a process group, make the stream current instead of passing it")

@@ -72,3 +72,18 @@ def test_a_step_on_another_stream_allocates_there(monkeypatch):
     assert {s for _, s in log} == {"side"}
     with pytest.raises(ValueError):
         ctx.train_step(theta, x, y, FakeOpt(ctx, [theta]), stream="side", group=object())
+
+
+def test_an_optimiser_of_other_parameters_is_refused():
+    log = []
+    ctx = Fake(log)
+    theta, x, y = case()
+    for params in ([theta.clone()], [theta, theta.clone()], [theta[:, :1]], [theta.view(-1)[1:]]):
+        opt = FakeOpt(ctx, params)
+        with pytest.raises(ValueError):
+            ctx.train_step(theta, x, y, opt)
+        assert not log and not opt.taken  # refused before anything ran
+    for same in (theta, theta.view(-1), theta.detach()):
+        opt = FakeOpt(ctx, [same])
+        E, loss, norm = ctx.train_step(theta, x, y, opt)
+        assert norm is None and torch.equal(opt.taken[0], theta / 2 + x.mean())
