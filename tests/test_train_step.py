@@ -87,3 +87,40 @@ def test_an_optimiser_of_other_parameters_is_refused():
         opt = FakeOpt(ctx, [same])
         E, loss, norm = ctx.train_step(theta, x, y, opt)
         assert norm is None and torch.equal(opt.taken[0], theta / 2 + x.mean())
+
+
+def _rank(rank, world, port, out):
+    import os
+
+    import torch.distributed as dist
+
+    os.environ["MASTER_ADDR"], os.environ["MASTER_PORT"] = "127.0.0.1", str(port)
+    dist.init_process_group("gloo", rank=rank, world_size=world)
+    try:
+        log = []
+        ctx = Fake(log)
+        theta, x, y = case()
+        x = x * (rank + 1)
+        taken = []
+        for group in (dist.group.WORLD, dist.new_group([0, 1]), None):
+            opt = FakeOpt(ctx, [theta])
+            ctx.train_step(theta, x, y, opt, group=group)
+            taken += opt.taken
+        torch.save(taken, f"{out}{rank}")
+    finally:
+        dist.destroy_process_group()
+
+
+def test_ranks_of_a_group_step_with_the_mean_gradient(tmp_path):
+    import torch.multiprocessing as mp
+
+    from test_multiprocess import _free_port
+
+    out = str(tmp_path / "taken")
+    mp.start_processes(_rank, args=(2, _free_port(), out), nprocs=2, start_method="spawn")
+    theta = case()[0]
+    for rank in range(2):
+        mean, pair, own = torch.load(f"{out}{rank}")
+        # theta / 2 + 1 on rank 0, theta / 2 + 2 on rank 1
+        assert torch.equal(mean, theta / 2 + 1.5) and torch.equal(pair, mean)
+        assert torch.equal(own, theta / 2 + 1 + rank)  # without a group every rank keeps its own
