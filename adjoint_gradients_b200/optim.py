@@ -275,16 +275,21 @@ class AdamW:
         return tuple(out)
 
     def state_dict(self) -> dict:
-        """Copies of the states, the master weights and the step count, for load_state."""
+        """Copies of the states, the master weights (None for tensors without) and the step
+        count, for load_state."""
         d = {"step": self.step_count, "m": self.m.clone(), "v": self.v.clone()}
         if self.state == "8bit":
             d |= {"m_scale": self.m_scale.clone(), "v_scale": self.v_scale.clone()}
-        if any(w is not None for w in self.master):
-            d["master"] = [None if w is None else w.clone() for w in self.master]
+        d["master"] = [None if w is None else w.clone() for w in self.master]
         return d
 
     def load_state(self, d: dict):
-        """Take the states and the step count of state_dict() (on the current stream)."""
+        """Take the states, the master weights and the step count of state_dict() (on the
+        current stream).  Parameters with master weights become their rounded copies; a
+        dict without "master" leaves those as they are.  One that does not fit is refused
+        (ValueError) and changes nothing."""
+        import torch
+
         have = {"m": self.m, "v": self.v, "m_scale": self.m_scale, "v_scale": self.v_scale}
         for key, mine in have.items():
             x = d.get(key)
@@ -292,10 +297,24 @@ class AdamW:
                 raise ValueError(f"{key}: states of another kind")
             if mine is not None and (x.shape != mine.shape or x.dtype != mine.dtype):
                 raise ValueError(f"{key}: states of other tensors")
-        for key, mine in have.items():
-            if mine is not None:
-                mine.copy_(d[key])
-        for mine, x in zip(self.master, d.get("master", [])):
-            if mine is not None and x is not None:
-                mine.copy_(x)
-        self.step_count = int(d["step"])
+        master = list(d.get("master", self.master))
+        if len(master) != len(self.master):
+            raise ValueError(f"master: {len(master)} tensors for {len(self.master)}")
+        for mine, x in zip(self.master, master):
+            if (x is None) != (mine is None):
+                raise ValueError("master: weights of a handle with other master weights")
+            if mine is not None and (x.shape != mine.shape or x.dtype != mine.dtype):
+                raise ValueError("master: weights of other tensors")
+        step = int(d["step"])
+        if step < 0:
+            raise ValueError("step: a count of steps")
+        with torch.no_grad():
+            for key, mine in have.items():
+                if mine is not None:
+                    mine.copy_(d[key])
+            if "master" in d:
+                for p, mine, x in zip(self.params, self.master, master):
+                    if mine is not None:
+                        mine.copy_(x)
+                        p.copy_(mine.view(p.shape))
+        self.step_count = step
