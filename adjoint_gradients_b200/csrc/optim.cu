@@ -839,9 +839,10 @@ __device__ __forceinline__ double chunk_squares(const GT* g, int count) {
   return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
-// Sum of squares in fp64 (an fp32 gradient's square neither overflows nor
-// underflows there), in a fixed order: per thread over the block's chunks,
-// the block, then all blocks' partials by the block that finishes last.
+// Sum of squares in a fixed order: per thread over the block's chunks (eight at
+// a time, see eight_squares(); element by element in fp64, where an fp32
+// gradient's square neither overflows nor underflows, if the wide loads cannot
+// take them), the block, then all blocks' partials by the block that finishes last.
 template <int CAP>
 __global__ void __launch_bounds__(kThreadsOpt)
     grad_norm_kernel(const __grid_constant__ OptNormArgs a, const __grid_constant__ GradPtrs<CAP> gp) {

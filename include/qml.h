@@ -552,8 +552,14 @@ QML_API qml_status qml_opt_get_step(qml_opt* opt, long long* t, void* stream);
  *   norm_dev  null, or a device float (fp64 parameters: double) for the norm
  *             before clipping; requires max_norm > 0
  * Without clipping, gradients that are not finite go through the formulas.
- * Sums of squares are in fp64 and in a fixed order: every result is
- * reproducible bit for bit. */
+ * Sums of squares run in a fixed order: two fp32 (four bf16 / fp16) squares
+ * are added in fp32 where their range allows it, everything else in fp64, so
+ * that the norm is within 2^-24 of its size (fp64: 2^-53) before it is rounded
+ * to its type.  Gradients off the wide loads' boundaries (32 bytes, bf16 /
+ * fp16 16) and handles of up to 65,536 elements in a clipped step add all in
+ * fp64.  The same call on gradients of the same alignment gives the same
+ * results bit for bit; the norm of another alignment or entry point may
+ * differ in its last bits, and with it what clipping makes of the step. */
 QML_API qml_status qml_opt_step(qml_opt* opt, const void* const* grads, double lr, const void* lr_dev,
                                 double grad_scale, double max_norm, void* norm_dev, void* stream);
 

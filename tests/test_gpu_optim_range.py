@@ -55,3 +55,25 @@ def test_a_first_moment_without_a_second_one_is_not_kept(n):
         assert (m[~first] == 0).all(), m[zero]
         # lr m / eps of the moments before rounding: 0.1 * 1e-24 / 1e-8 a step, nothing in fp32
         assert (p.cpu().numpy()[~first] == 1.0).all()
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16", "fp64"])
+@pytest.mark.parametrize("n", [5000, 65_536, 300_007])
+def test_the_norm_whatever_the_gradients_alignment(dtype, n):
+    # fp32: of two squares' sum, each of two operations is off by u = 2^-24 of it at most,
+    # four exact 16-bit squares' by two sums, so the root by u; then its own rounding, u.
+    # The fp64 sums of n terms add n 2^-53 (fp64: each of the squares' roundings among them).
+    types = {"fp32": torch.float32, "bf16": torch.bfloat16, "fp16": torch.float16, "fp64": torch.float64}
+    gen = torch.Generator("cuda").manual_seed(n)
+    x = (torch.randn(n, generator=gen, device="cuda", dtype=torch.float64) * 0.1).to(types[dtype])
+    want = float((x.cpu().numpy().astype(np.longdouble) ** 2).sum() ** np.longdouble(0.5)) if dtype in ("fp32", "fp64") \
+        else float(x.double().square().sum().sqrt())
+    bound = (0 if dtype == "fp64" else 2 * 2.0 ** -24) + (n + 2) * 2.0 ** -53
+    for shift in (0, 1, 3):
+        buf = torch.empty(n + 8, dtype=types[dtype], device="cuda")
+        g = buf[shift:shift + n].copy_(x)
+        opt = optim().AdamW([torch.zeros(n, dtype=types[dtype], device="cuda")])
+        got = [float(opt.grad_norm([g])), float(opt.step([g], max_norm=1.0)), float(opt.step([g], max_norm=float("inf")))]
+        again = [float(opt.grad_norm([g])), float(opt.step([g], max_norm=1.0)), float(opt.step([g], max_norm=float("inf")))]
+        assert got == again
+        assert all(abs(x - want) <= bound * want for x in got), (shift, got, want)
