@@ -305,46 +305,38 @@ cudaError_t launch_slot8_copy(bool save, float2* psi, int8_t* codes, uint8_t* ex
   const long long count = (long long)B << n;
   if (n < 4) {
     const unsigned g = (unsigned)((B + 63) / 64);
-    if (save) launch_after(slot8_small_kernel<0>, g, 64, 1, s, psi, nullptr, codes, exps, nullptr, B, 1 << n);
-    else launch_after(slot8_small_kernel<1>, g, 64, 1, s, psi, nullptr, codes, exps, nullptr, B, 1 << n);
-    return cudaGetLastError();
+    if (save) return launch_after(slot8_small_kernel<0>, g, 64, 1, s, psi, nullptr, codes, exps, nullptr, B, 1 << n);
+    return launch_after(slot8_small_kernel<1>, g, 64, 1, s, psi, nullptr, codes, exps, nullptr, B, 1 << n);
   }
   if (cb > kTileBits) return cudaErrorInvalidValue;
   const BitMap m = bit_map(cb, to);
   const unsigned g = (unsigned)((count + (long long)kWarpAmps * (kThreads8 / 32) - 1) / ((long long)kWarpAmps * (kThreads8 / 32)));
   if (save) {
-    if (cb) launch_after(slot8_save_kernel<true>, g, kThreads8, 1, s, psi, codes, exps, count, m);
-    else launch_after(slot8_save_kernel<false>, g, kThreads8, 1, s, psi, codes, exps, count, m);
-  } else {
-    if (cb) launch_after(slot8_load_kernel<true>, g, kThreads8, 1, s, psi, codes, exps, count, m);
-    else launch_after(slot8_load_kernel<false>, g, kThreads8, 1, s, psi, codes, exps, count, m);
+    if (cb) return launch_after(slot8_save_kernel<true>, g, kThreads8, 1, s, psi, codes, exps, count, m);
+    return launch_after(slot8_save_kernel<false>, g, kThreads8, 1, s, psi, codes, exps, count, m);
   }
-  return cudaGetLastError();
+  if (cb) return launch_after(slot8_load_kernel<true>, g, kThreads8, 1, s, psi, codes, exps, count, m);
+  return launch_after(slot8_load_kernel<false>, g, kThreads8, 1, s, psi, codes, exps, count, m);
 }
 
 cudaError_t launch_slot8_from_planes(const float2* buf, const float2* partner, int8_t* codes, uint8_t* exps, int B,
                                      int n, cudaStream_t s) {
   if (n < 4) {
-    launch_after(slot8_small_kernel<2>, (unsigned)((B + 63) / 64), 64, 1, s, const_cast<float2*>(buf),
-                                                                   const_cast<float2*>(partner), codes, exps, nullptr,
-                                                                   B, 1 << n);
-    return cudaGetLastError();
+    return launch_after(slot8_small_kernel<2>, (unsigned)((B + 63) / 64), 64, 1, s, const_cast<float2*>(buf),
+                        const_cast<float2*>(partner), codes, exps, nullptr, B, 1 << n);
   }
   const dim3 g(blocks_for(1ll << n), (unsigned)((B + 1) / 2 < 32768 ? (B + 1) / 2 : 32768));
-  launch_after(slot8_from_planes_kernel, g, kThreads8, 1, s, buf, partner, codes, exps, B, 1ll << n);
-  return cudaGetLastError();
+  return launch_after(slot8_from_planes_kernel, g, kThreads8, 1, s, buf, partner, codes, exps, B, 1ll << n);
 }
 
 cudaError_t launch_slot8_to_planes(float2* plane0, float2* plane1, const int8_t* codes, const uint8_t* exps,
                                    const float* rscale, int B, int n, cudaStream_t s) {
   if (n < 4) {
-    launch_after(slot8_small_kernel<3>, (unsigned)((B + 63) / 64), 64, 1, s, plane0, plane1, const_cast<int8_t*>(codes),
-                                                                   const_cast<uint8_t*>(exps), rscale, B, 1 << n);
-    return cudaGetLastError();
+    return launch_after(slot8_small_kernel<3>, (unsigned)((B + 63) / 64), 64, 1, s, plane0, plane1,
+                        const_cast<int8_t*>(codes), const_cast<uint8_t*>(exps), rscale, B, 1 << n);
   }
   const long long count = (long long)B << n;
-  launch_after(slot8_to_planes_kernel, blocks_for(count), kThreads8, 1, s, plane0, plane1, codes, exps, rscale, count);
-  return cudaGetLastError();
+  return launch_after(slot8_to_planes_kernel, blocks_for(count), kThreads8, 1, s, plane0, plane1, codes, exps, rscale, count);
 }
 
 }  // namespace qml

@@ -10,6 +10,8 @@ namespace qml {
 // after_previous() before its first access to memory that another kernel
 // writes.  In a row of small
 // kernels this hides most of a launch.  cluster: blocks of a cluster (1: none).
+// The result is this launch's own: an error that another call left in the
+// runtime (cudaGetLastError) is none of it.
 template <class... P, class... A>
 cudaError_t launch_after(void (*kernel)(P...), dim3 grid, unsigned threads, unsigned cluster, cudaStream_t s,
                          A&&... args) {
@@ -24,7 +26,9 @@ cudaError_t launch_after(void (*kernel)(P...), dim3 grid, unsigned threads, unsi
   cfg.stream = s;
   cfg.attrs = at;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+  if (e != cudaSuccess) cudaGetLastError();  // returned, not left behind for the thread's next call
+  return e;
 }
 
 // Waits until the previous kernel of the stream has finished and its writes are

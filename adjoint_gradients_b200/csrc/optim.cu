@@ -891,6 +891,7 @@ __global__ void __launch_bounds__(kThreadsOpt)
 }
 
 __global__ void opt_set_kernel(OptCtrl* c, long long t, double log_b1, double log_b2, unsigned long long seed) {
+  after_previous();
   set_counter(c, t, log_b1, log_b2, seed);
 }
 
@@ -899,8 +900,7 @@ template <class F>
 cudaError_t with_ptrs(const void* const* grads, int n, F&& f) {
   auto fill = [&](auto& gp) {
     for (int i = 0; i < n; ++i) gp.p[i] = grads[i];
-    f(gp);
-    return cudaGetLastError();
+    return f(gp);
   };
   if (n <= kOptCaps[0]) {
     GradPtrs<kOptCaps[0]> gp;
@@ -965,21 +965,20 @@ cudaError_t step_combo(bool bits8, const OptSettings& t, const OptClipArgs* smal
         const int blocks = std::min(grid, small->cluster), warps = (grid + blocks - 1) / blocks;
         if constexpr (sizeof(PT) < 8) {
           if (bits8) {
-            launch_after(adamw_small_kernel<PT, GT, C, MASTER, true, CAP>, blocks, warps * 32, blocks, s, a, *small, gp);
-            return;
+            return launch_after(adamw_small_kernel<PT, GT, C, MASTER, true, CAP>, blocks, warps * 32, blocks, s, a, *small,
+                                gp);
           }
         }
-        launch_after(adamw_small_kernel<PT, GT, C, MASTER, false, CAP>, blocks, warps * 32, blocks, s, a, *small, gp);
-        return;
+        return launch_after(adamw_small_kernel<PT, GT, C, MASTER, false, CAP>, blocks, warps * 32, blocks, s, a, *small,
+                            gp);
       }
     }
     if constexpr (sizeof(PT) < 8) {
       if (bits8) {
-        launch_after(adamw_kernel<PT, GT, C, MASTER, true, CAP>, grid, kThreadsOpt, 1, s, a, gp);
-        return;
+        return launch_after(adamw_kernel<PT, GT, C, MASTER, true, CAP>, grid, kThreadsOpt, 1, s, a, gp);
       }
     }
-    launch_after(adamw_kernel<PT, GT, C, MASTER, false, CAP>, grid, kThreadsOpt, 1, s, a, gp);
+    return launch_after(adamw_kernel<PT, GT, C, MASTER, false, CAP>, grid, kThreadsOpt, 1, s, a, gp);
   });
 }
 
@@ -1028,14 +1027,13 @@ int opt_cluster_limit(const OptCombo& c) {
 cudaError_t launch_opt_norm(const OptNormArgs& a, const void* const* grads, int n, int grid, cudaStream_t s) {
   return with_ptrs(grads, n, [&](auto& gp) {
     constexpr int CAP = sizeof(gp.p) / sizeof(gp.p[0]);
-    launch_after(grad_norm_kernel<CAP>, grid, kThreadsOpt, 1, s, a, gp);
+    return launch_after(grad_norm_kernel<CAP>, grid, kThreadsOpt, 1, s, a, gp);
   });
 }
 
 cudaError_t launch_opt_set(OptCtrl* ctrl, long long t, double beta1, double beta2, unsigned long long seed,
                            cudaStream_t s) {
-  opt_set_kernel<<<1, 1, 0, s>>>(ctrl, t, std::log(beta1), std::log(beta2), seed);
-  return cudaGetLastError();
+  return launch_after(opt_set_kernel, 1, 1, 1, s, ctrl, t, std::log(beta1), std::log(beta2), seed);
 }
 
 }  // namespace qml

@@ -281,6 +281,11 @@ qml_status qml_opt_set_workspace(qml_opt* o, void* ws, size_t bytes, void* strea
   if (bytes < o->bytes()) return QML_ERR_WORKSPACE;
   DeviceGuard g(o->device);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int now = -1;
+  if (cudaGetDevice(&now) != cudaSuccess || now != o->device) {  // the handle's device is not there
+    cudaGetLastError();
+    return QML_ERR_CUDA;
+  }
   o->ws = static_cast<char*>(ws);
   if (o->small) {
     o->cluster = opt_cluster_limit(o->launches[0].combo);
