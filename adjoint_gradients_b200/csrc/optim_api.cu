@@ -48,7 +48,10 @@ size_t type_size(int t) { return t == QML_F64 ? 8 : t == QML_F32 ? 4 : 2; }
 
 bool off(const void* p, size_t a) { return ((uintptr_t)p) % a != 0; }
 
-bool negative_or_not_finite(double x) { return !(x >= 0.0) || !std::isfinite(x); }
+// Whether a factor is finite in the type that the step computes in.
+bool finite_in(bool f64, double x) { return std::isfinite(f64 ? x : (double)(float)x); }
+
+bool negative_or_not_finite(bool f64, double x) { return !(x >= 0.0) || !finite_in(f64, x); }
 
 // Tensors of one launch: one combination of types, at most as many as the
 // kernel parameters hold gradient pointers.
@@ -93,7 +96,8 @@ qml_status check_tensor(const qml_opt_tensor& t, bool bits8, std::vector<std::pa
   if (t.grad_dtype != t.dtype && !(half && t.grad_dtype == QML_F32)) return QML_ERR_UNSUPPORTED;
   if (t.dtype == QML_F64 && bits8) return QML_ERR_UNSUPPORTED;
   if (t.master && !half) return QML_ERR_UNSUPPORTED;
-  if (negative_or_not_finite(t.lr_scale) || negative_or_not_finite(t.weight_decay)) return QML_ERR_INVALID_ARG;
+  const bool f64 = t.dtype == QML_F64;
+  if (negative_or_not_finite(f64, t.lr_scale) || negative_or_not_finite(f64, t.weight_decay)) return QML_ERR_INVALID_ARG;
   if (t.numel < 0 || t.numel > kMaxElements) return QML_ERR_INVALID_ARG;
   if (t.numel == 0) return QML_OK;
   const size_t n = (size_t)t.numel, ps = type_size(t.dtype);
@@ -328,7 +332,7 @@ qml_status qml_opt_step(qml_opt* o, const void* const* grads, double lr, const v
                         double max_norm, void* norm_dev, void* stream) {
   qml_status st = ready(o, grads, grad_scale);
   if (st != QML_OK) return st;
-  if (!lr_dev && negative_or_not_finite(lr)) return QML_ERR_INVALID_ARG;
+  if (!finite_in(o->f64, grad_scale) || (!lr_dev && negative_or_not_finite(o->f64, lr))) return QML_ERR_INVALID_ARG;
   const size_t real = o->f64 ? 8 : 4;
   if (off(lr_dev, real) || off(norm_dev, real)) return QML_ERR_INVALID_ARG;
   if (!(max_norm >= 0.0) || (norm_dev && max_norm == 0.0)) return QML_ERR_INVALID_ARG;

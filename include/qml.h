@@ -499,7 +499,7 @@ typedef struct {
   long long numel;     /* 0 .. 2^36 (all tensors together, too); 0 takes null pointers */
   int dtype;           /* qml_dtype of param */
   int grad_dtype;      /* dtype, or QML_F32 for bf16 / fp16 params */
-  double lr_scale;     /* >= 0 */
+  double lr_scale;     /* >= 0, finite in the arithmetic's type (this and every other factor) */
   double weight_decay; /* >= 0 */
 } qml_opt_tensor;
 

@@ -68,3 +68,20 @@ def test_a_device_that_is_not_there_is_refused_before_anything_is_written():
     lib.qml_opt_destroy(h)
     torch.cuda.synchronize()
     assert bool((ws == 5).all())
+
+
+def test_factors_beyond_the_arithmetics_type_are_refused():
+    for dtype, refused in (("fp32", True), ("bf16", True), ("fp64", False)):
+        params, grads = make([300], dtype, dtype, 51)
+        opt = optim().AdamW(params, weight_decay=0.0)
+        before = bits(params + [opt.m, opt.v])
+        for kw in (dict(lr=1e39), dict(grad_scale=1e39), dict(grad_scale=-1e39, max_norm=1.0)):
+            if not refused:
+                opt.step(grads, **kw)
+                continue
+            with pytest.raises(qml().QmlError) as e:
+                opt.step(grads, **kw)
+            assert e.value.code == 1
+        assert opt.step_count == (0 if refused else 3)
+        assert same(before, bits(params + [opt.m, opt.v])) == refused
+        assert bool(torch.isfinite(params[0]).all())
