@@ -134,6 +134,8 @@ class AdamW:
         self._capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)
         self._on_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
         self._numels, self._dtypes = [p.numel() for p in params], gt
+        self._written = params + [w for w in self.master if w is not None]
+        self._increment_version = getattr(torch._C, "_increment_version", torch.autograd.graph.increment_version)
         nbytes = int(self.lib.qml_opt_workspace_bytes(h))
         self.ws = torch.empty(nbytes + 256, dtype=torch.uint8, device=self.device)
         qml._check(self.lib.qml_opt_set_workspace(h, (self.ws.data_ptr() + 255) // 256 * 256, nbytes, self._stream(None)),
@@ -232,6 +234,7 @@ class AdamW:
             norm_ptr = norm.data_ptr()
         qml._check(self.lib.qml_opt_step(self._h, self._take(grads), lr, lr_dev, grad_scale, max_norm, norm_ptr,
                                          self._stream(stream)), "qml_opt_step")
+        self._increment_version(self._written)  # so that autograd notices tensors saved before the step
         return norm
 
     def grad_norm(self, grads, grad_scale: float = 1.0, norm=None, stream=None):
