@@ -1723,9 +1723,9 @@ qml_status qml_sync(qml_ctx* c, void* stream) {
   DeviceGuard g(c->device);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   unsigned word = 0;
-  cudaError_t e = cudaStreamSynchronize(s);
-  if (e == cudaSuccess) e = cudaMemcpy(&word, c->ws + c->lay.status, sizeof(word), cudaMemcpyDeviceToHost);
-  if (e == cudaSuccess) e = cudaMemset(c->ws + c->lay.status, 0, sizeof(word));
+  cudaError_t e = cudaMemcpyAsync(&word, c->ws + c->lay.status, sizeof(word), cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e == cudaSuccess) e = cudaMemsetAsync(c->ws + c->lay.status, 0, sizeof(word), s);
   if (e != cudaSuccess) return QML_ERR_CUDA;
   for (int code = 1; code < 32; ++code)
     if (word & (1u << code)) return static_cast<qml_status>(code);

@@ -323,8 +323,9 @@ qml_status qml_opt_get_step(qml_opt* o, long long* t, void* stream) {
   if (!o || !t) return QML_ERR_INVALID_ARG;
   if (!o->ws) return QML_ERR_WORKSPACE;
   DeviceGuard g(o->device);
-  cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
-  if (e == cudaSuccess) e = cudaMemcpy(t, &o->ctrl()->t, sizeof(*t), cudaMemcpyDeviceToHost);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaMemcpyAsync(t, &o->ctrl()->t, sizeof(*t), cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   return e == cudaSuccess ? QML_OK : QML_ERR_CUDA;
 }
 
@@ -384,10 +385,13 @@ qml_status qml_opt_sync(qml_opt* o, void* stream) {
   if (!o) return QML_ERR_INVALID_ARG;
   if (!o->ws) return QML_ERR_WORKSPACE;
   DeviceGuard g(o->device);
+  // all on `stream`: on the default stream the clearing could come after a later
+  // call's error, and wait for work that is none of this handle's
   unsigned word = 0;
-  cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
-  if (e == cudaSuccess) e = cudaMemcpy(&word, &o->ctrl()->status, sizeof(word), cudaMemcpyDeviceToHost);
-  if (e == cudaSuccess && word) e = cudaMemset(&o->ctrl()->status, 0, sizeof(word));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaMemcpyAsync(&word, &o->ctrl()->status, sizeof(word), cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e == cudaSuccess && word) e = cudaMemsetAsync(&o->ctrl()->status, 0, sizeof(word), s);
   if (e != cudaSuccess) return QML_ERR_CUDA;
   for (int code = 1; code < 32; ++code)
     if (word & (1u << code)) return static_cast<qml_status>(code);

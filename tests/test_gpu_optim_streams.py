@@ -94,3 +94,32 @@ def test_training_steps_on_another_stream(n, L, B, handle):
         runs.append(bits([th, opt.m, opt.v] + [t for o in outs for t in o]))
     assert same(*runs)
     assert len(noise) == 15
+
+
+def test_reading_the_status_is_the_given_streams_business():
+    # on the default stream the clearing of the status word could follow a later call's
+    # error on another one; shown by the default stream's work, which nothing waits for
+    params, grads = make([24, 5003], "fp32", "fp32", 33)
+    opt = optim().AdamW(params)
+    ctx = qml().Context(4, 2, 3)
+    grads[1][7] = math.nan
+    side = torch.cuda.Stream()
+    opt.step(grads, max_norm=1.0, stream=side)  # (what the first call sets up waits, too)
+    side.synchronize()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(2_000_000_000)  # about a second
+    busy = torch.cuda.Event()
+    busy.record()
+    opt.step(grads, max_norm=1.0, stream=side)
+    with pytest.raises(qml().QmlError) as e:
+        opt.sync(side)
+    assert e.value.code == 6
+    opt.step(grads, max_norm=1.0, stream=side)
+    with pytest.raises(qml().QmlError) as e:
+        opt.sync(side)
+    opt.sync(side)
+    ctx.sync(side)
+    with torch.cuda.stream(side):
+        assert opt.step_count == 0
+    assert not busy.query()
+    torch.cuda.synchronize()
