@@ -193,7 +193,8 @@ __global__ void __launch_bounds__(kThreads8)
 // A slot from the forward pass's working layout: unit u = samples 2u, 2u + 1
 // keeps (Re, Re) of the two at sample 2u's positions and (Im, Im) at sample
 // 2u + 1's (an odd batch's last unit: in `partner`).  Four addresses of a unit
-// a lane; grid.y: units.
+// a lane; grid.y: units.  Bound by memory with one run a warp: 20 qubits x 32 54
+// us, where the save kernel with its four takes 51 (ncu).
 __global__ void __launch_bounds__(kThreads8)
     slot8_from_planes_kernel(const float2* buf, const float2* partner, int8_t* codes, uint8_t* exps, int B,
                              long long N) {
@@ -231,7 +232,8 @@ __global__ void __launch_bounds__(kThreads8)
 }
 
 // The psi lanes of the backward planes from a slot, times *rscale (null: 1):
-// plane0[i].x = Re, plane1[i].x = Im.
+// plane0[i].x = Re, plane1[i].x = Im.  The planes are read and written whole, 34
+// bytes an amplitude: 20 qubits x 32 185 us (ncu), 6.2 TB/s.
 __global__ void __launch_bounds__(kThreads8)
     slot8_to_planes_kernel(float2* plane0, float2* plane1, const int8_t* codes, const uint8_t* exps,
                            const float* rscale, long long count) {

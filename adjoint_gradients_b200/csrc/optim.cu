@@ -187,7 +187,8 @@ __device__ __forceinline__ void st8(T* p, const C (&x)[8]) {
 
 // ------------------------------------------------------------ random rounding
 
-// 32-bit integer mixer: xorshifts and two odd multipliers.  An element's two
+// 32-bit integer mixer: xorshifts and two odd multipliers, whose constants C.
+// Wellons published in 2018 as the result of a search for low bias.  An element's two
 // random numbers are the low and the high half of mix(): from the value before
 // its last step, y, these are the low half xor the high half, and the high half.
 __device__ __forceinline__ uint32_t mix_most(uint32_t x) {
@@ -549,9 +550,10 @@ __device__ __forceinline__ bool takes_wide(const OptChunk& c, const GT* g) {
 // The general step: a block a unit of work, a warp a block of 256 elements a
 // round.  Full states are bound by memory (128M fp32 elements, 28 bytes each:
 // 526 us, 6.8 TB/s, above the rate of a plain copy).  8-bit states are bound by
-// the instructions they issue, some 70 an element of which the rounding takes
-// 25, its random bits 9 and the exactly rounded root 10 (128M: 384 us, 5.4 TB/s;
-// 315 us without these three).  Three blocks an SM: 80 registers.
+// the instructions they issue, some 72 an element of which the rounding takes
+// 26, its random bits 9 and the exactly rounded root 10 (128M: 385 us, 5.3 TB/s;
+// 315 us without these three).  Three blocks an SM: 80 registers.  fp64 takes 178
+// registers, one block an SM, and waits for memory (48M elements 442 us, 6.1 TB/s).
 template <class PT, class GT, class C, bool MASTER, bool S8, int CAP>
 __global__ void __launch_bounds__(kThreadsOpt, sizeof(C) == 4 ? 3 : 1)
     adamw_kernel(const __grid_constant__ OptStepArgs<C> a, const __grid_constant__ GradPtrs<CAP> gp) {

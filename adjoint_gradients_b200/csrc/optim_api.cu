@@ -24,8 +24,10 @@ constexpr int kNormPerSm = 4;  // blocks of the norm's launches, per SM: as many
 // record, the step's factors, the random key, the unit's scales: some 2 us of
 // dependent loads), so units are as long as leaves one for every block that is
 // resident at once (3 an SM), or a whole number of them, up to a cap.  128M fp32
-// elements with 1 / 2 / 4 / 8 / 16 rounds: 8-bit 746 / 494 / 419 / 389 / 385
-// us; full states, whose start is shorter, 611 / 537 / 526 / 538 / 544.
+// elements with 1 / 2 / 4 / 8 / 16 rounds (the 8-bit kernel as it was then): 8-bit
+// 746 / 494 / 419 / 389 / 385 us; full states, whose start is shorter, 611 / 537 /
+// 526 / 538 / 544.  fp64 has one block an SM, its units are cut for three all the
+// same: no other number has been measured (4M elements 47 us, floor 34).
 constexpr long long kResident = 148 * 3;
 int rounds_for(long long total, bool bits8) {
   const long long rounds = (total + kOptChunk - 1) / kOptChunk, cap = bits8 ? kOptMaxRounds : 4;
@@ -37,7 +39,8 @@ int rounds_for(long long total, bool bits8) {
 // Device time a step, one launch against the general kernels (clipped: two
 // launches), full / 8-bit states: 60,000 fp32 elements 3.2 / 3.9 against 3.8 /
 // 4.7 us, clipped 4.1 / 4.9 against 7.8 / 8.5; 6,000 clipped 3.3 against 8.1.
-// (fp64, 60,000, not clipped: 5.9 against 5.5.)
+// fp64 at 60,000 loses a little where the step is not clipped, 5.9 against 5.5:
+// the units are cut when the handle is made, before it is known whether it will be.
 constexpr long long kSmallBlocks = kOptSmallCluster * kOptSmallWarps;
 
 constexpr long long kMaxElements = 1ll << 36;  // of a handle: what 180 GB of states cannot hold
