@@ -123,3 +123,21 @@ def test_reading_the_status_is_the_given_streams_business():
         assert opt.step_count == 0
     assert not busy.query()
     torch.cuda.synchronize()
+
+
+def test_the_default_stream_given_while_another_is_current():
+    n, L, B = 6, 3, 5
+    x, theta, y = (torch.from_numpy(a.astype(np.float32)).cuda() for a in random_case(89, B, n, L))
+    torch.cuda.synchronize()
+    runs = []
+    for stream in (None, 0, torch.cuda.default_stream()):
+        ctx = qml().Context(n, L, B, ckpt_block=1)
+        th = theta.clone()
+        opt = optim().AdamW([th], lr=0.05)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(torch.cuda.current_stream() if stream is None else torch.cuda.Stream()):
+            outs = [ctx.train_step(th, x, y, opt, max_norm=0.5, stream=stream) for _ in range(3)]
+            outs.append((opt.grad_norm([theta], stream=stream),))
+            torch.cuda.synchronize()
+            runs.append(bits([th, opt.m, opt.v] + [t for o in outs for t in o]))
+    assert same(*runs[:2]) and same(*runs[1:])
